@@ -856,7 +856,8 @@ struct CoreF32 {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             // a key that this column does not see weighs nothing, also where its step is NaN
-                            const bool none = CUT && e[c] == 0.f;
+                            // (one that it sees may weigh 0 too: then NaN is NaN)
+                            const bool none = CUT && sc[nt][kb][h][c] == -INFINITY;
                             w[c] = none ? 0.f : e[c] * s[gr];
                             zs[nt][c][gr] = none ? zs[nt][c][gr] : fmaf(e[c], z[gr], zs[nt][c][gr]);
                         }
