@@ -108,16 +108,22 @@ struct Terms {
 };
 
 // Products of two 16-deep steps (8 channels per lane) of split operands: the
-// terms whose weights add up to less than 2^-24 of the product are left out
+// terms whose weights add up to less than 2^-24 of the product are left out.
+// The matrix instructions cut their sums instead of rounding them to nearest:
+// over a long chain that shows in the fifth digit.  So the steps are summed by
+// themselves, smallest terms first, and added in fp32.
 __device__ __forceinline__ void mma_steps(float (&d)[4], const uint32_t (&a0)[3][4], const uint32_t (&a1)[3][4],
                                           const uint32_t (&b)[3][4]) {
+    float part[4] = {};
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int w = 2; w >= 0; --w)
 #pragma unroll
-        for (int j = 0; i + j < 3; ++j)
+        for (int i = 0; i <= w; ++i)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                mma_bf16(d, a0[i][2 * s], a1[i][2 * s], a0[i][2 * s + 1], a1[i][2 * s + 1], b[j][2 * s], b[j][2 * s + 1]);
+                mma_bf16(part, a0[i][2 * s], a1[i][2 * s], a0[i][2 * s + 1], a1[i][2 * s + 1], b[w - i][2 * s], b[w - i][2 * s + 1]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] += part[e];
 }
 
 // bf16: h of a tile's rows x 64 ranks over one slice of d.  Ranks are the m of
