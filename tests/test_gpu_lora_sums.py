@@ -37,7 +37,7 @@ def _error(dtype, M, d, n, rank, room, mean=0.0, seed=0):
     (20, 13824, 1024, 128, 2),
 ])
 @pytest.mark.parametrize("mean", [0.0, 0.5])      # signs that cancel, and sums that grow
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_lora_sums_are_those_of_fp32(M, d, n, rank, room, mean, dtype):
     """Relative to a row's norm.  The matrix instructions cut what lies below an fp32 accumulator's last place: at most
     2^-23 of it each, half of that on average.  16 in a row, the accumulator growing evenly from nothing: 8 x 2^-23 = 2^-20
