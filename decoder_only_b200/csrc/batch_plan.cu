@@ -73,13 +73,14 @@ __device__ __forceinline__ int above(const T* ends, int n, int x) {
 // adapter's rows.  Per request: first[b], its first position less its first
 // row, and lora[b], the place of its first row (-1 without adapter).
 __device__ __forceinline__ void fill_row(const llama_batch_plan& p, const int* cu, const int* first, const int* lora,
-                                         int r, int rows, int lora_rows) {
+                                         int r, int rows, int lora_rows, int* err) {
     int seq = -1, pos = -1, slot = -1;
     if (r < rows) {
         seq = above(cu + 1, p.B, r);
         pos = first[seq] + r;
         const int page = *(volatile const int*)(p.d_table + (int64_t)seq * p.pages_per_seq + pos / kv4::PAGE);
         if (page >= 0 && page < p.n_pages) slot = page * kv4::PAGE + pos % kv4::PAGE;
+        else atomicOr(err, LLAMA_DEVERR_INPUT);
         if (p.n_adapters > 0 && lora[seq] >= 0) p.d_lora_rows[lora[seq] + r - cu[seq]] = r;
     }
     p.d_slots[r] = slot;
@@ -91,7 +92,7 @@ __device__ __forceinline__ void fill_row(const llama_batch_plan& p, const int* c
 // d_work of the plan: [0] rows, [1] rows with an adapter, then first[B] and
 // lora[B] of fill_row (kept here and not read again from d_past, which may be
 // the buffer that d_kv_len writes: the lengths of the next step)
-__global__ void __launch_bounds__(THREADS) batch_plan_kernel(const __grid_constant__ llama_batch_plan p, int fused) {
+__global__ void __launch_bounds__(THREADS) batch_plan_kernel(const __grid_constant__ llama_batch_plan p, int fused, int* err) {
     extern __shared__ int dyn[];                 // [warps in use][n_adapters] rows per (warp, adapter)
     __shared__ uint2 part[WARPS];
     __shared__ int cu[THREADS + 1], page_end[THREADS], held_of[THREADS], lora[THREADS], first[THREADS];
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const __grid_consta
         if (A > 0) adapter = p.d_adapter[t];
         right = past >= 0 && fresh >= 0 && (int64_t)past + fresh <= (int64_t)p.pages_per_seq * kv4::PAGE;
     }
-    const int n_free = min(max(*p.d_n_free, 0), p.free_capacity);
+    const int told = *p.d_n_free, n_free = min(max(told, 0), p.free_capacity);
+    if ((t < B && !right) || told != n_free) atomicOr(err, LLAMA_DEVERR_INPUT);
     const int held = right ? (int)(((unsigned)past + kv4::PAGE - 1) / kv4::PAGE) : 0;
     int n = right ? fresh : 0;
     int need = right ? (int)(((unsigned)(past + fresh) + kv4::PAGE - 1) / kv4::PAGE) - held : 0;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const __grid_consta
     if (t == 0) *p.d_n_free_out = n_free - pages;      // may be d_n_free itself: read by every thread above
     if (fused) {
         __syncthreads();                               // the table's new entries
-        for (int r = t; r < p.max_rows; r += THREADS) fill_row(p, cu, first, lora, r, rows, total_lora);
+        for (int r = t; r < p.max_rows; r += THREADS) fill_row(p, cu, first, lora, r, rows, total_lora, err);
     } else {
         if (t < B) {
             p.d_work[2 + t] = first[t];
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const __grid_consta
 
 constexpr int ROW_THREADS = 256;
 
-__global__ void __launch_bounds__(ROW_THREADS) plan_rows_kernel(const __grid_constant__ llama_batch_plan p) {
+__global__ void __launch_bounds__(ROW_THREADS) plan_rows_kernel(const __grid_constant__ llama_batch_plan p, int* err) {
     __shared__ int cu[THREADS + 1], first[THREADS], lora[THREADS];
     pdl_launch_dependents();
     pdl_wait();
@@ -232,12 +234,12 @@ __global__ void __launch_bounds__(ROW_THREADS) plan_rows_kernel(const __grid_con
     const int rows = p.d_work[0], lora_rows = p.d_work[1];
     __syncthreads();
     for (int r = blockIdx.x * ROW_THREADS + threadIdx.x; r < p.max_rows; r += gridDim.x * ROW_THREADS)
-        fill_row(p, cu, first, lora, r, rows, lora_rows);
+        fill_row(p, cu, first, lora, r, rows, lora_rows, err);
 }
 
 }  // namespace
 
-int launch_batch_plan(const llama_batch_plan& p, cudaStream_t st) {
+int launch_batch_plan(const llama_batch_plan& p, int* err, cudaStream_t st) {
     const int fused = p.max_rows <= FUSED_ROWS;
     const size_t smem = (size_t)((p.B + 31) / 32) * p.n_adapters * sizeof(int);    // 64 KB at the limits
     static PerDeviceOnce once;
@@ -247,10 +249,10 @@ int launch_batch_plan(const llama_batch_plan& p, cudaStream_t st) {
         return (int)LLAMA_OK;
     });
     if (rc) return rc;
-    launch_pdl(batch_plan_kernel, dim3(1), dim3(THREADS), smem, st, p, fused);
+    launch_pdl(batch_plan_kernel, dim3(1), dim3(THREADS), smem, st, p, fused, err);
     LLAMA_LAUNCH_CHECK();
     if (!fused) {
-        launch_pdl(plan_rows_kernel, dim3(ceil_div(p.max_rows, ROW_THREADS)), dim3(ROW_THREADS), 0, st, p);
+        launch_pdl(plan_rows_kernel, dim3(ceil_div(p.max_rows, ROW_THREADS)), dim3(ROW_THREADS), 0, st, p, err);
         LLAMA_LAUNCH_CHECK();
     }
     return LLAMA_OK;

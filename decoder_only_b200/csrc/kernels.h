@@ -135,7 +135,7 @@ int tc_num_sms();
 int gemm_tc_prepare();  // sets kernel attributes; call before any stream capture
 
 // batch_plan.cu
-int launch_batch_plan(const llama_batch_plan& p, cudaStream_t st);
+int launch_batch_plan(const llama_batch_plan& p, int* err, cudaStream_t st);
 
 // kv4_store.cu  (4-bit paged cache; n_slots = 128 * pages)
 int launch_kv4_append(int dtype, const void* k, const void* v, const int32_t* slots, uint8_t* pool, int rows, int n_kv,

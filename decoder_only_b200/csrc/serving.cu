@@ -42,7 +42,10 @@ int llama_op_batch_plan(const llama_batch_plan* plan, void* stream) {
     if (p.n_adapters > 0 && (!p.d_adapter || !p.d_lora_rows || !p.d_lora_tiles || !aligned16(p.d_lora_tiles) || !p.d_n_tiles ||
                              p.max_tiles < tiles))
         return LLAMA_ERR_INVALID_ARG;
-    return launch_batch_plan(p, (cudaStream_t)stream);
+    int* err = nullptr;
+    int rc = op_error_word(&err);
+    if (rc) return rc;
+    return launch_batch_plan(p, err, (cudaStream_t)stream);
 }
 
 uint64_t llama_kv4_pool_bytes(int32_t n_pages, int32_t n_kv, int32_t head_dim) {

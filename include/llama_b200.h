@@ -486,7 +486,10 @@ typedef struct llama_batch_plan {
  * changes for them).  An admitted request gets pages ceil(past / 128) ..
  * ceil((past + new) / 128) - 1 in its table row; the other entries are left
  * as they were.  kv_len = past + new if admitted, past if held back, 0 if
- * invalid.  A row whose page is outside the pool gets slot -1. */
+ * invalid.  A row whose page (its table entry, or one from the free list) is
+ * outside the pool gets slot -1.  Invalid requests, such rows and an n_free
+ * outside 0 .. free_capacity (taken as the nearer end) are recorded in the op
+ * error word. */
 LLAMA_API int llama_op_batch_plan(const llama_batch_plan* plan, void* stream);
 
 /* [NAR] "GQA Was Not an Original LLaMA Feature" (the KV cache and its bytes,
