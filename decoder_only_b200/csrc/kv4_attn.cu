@@ -339,8 +339,9 @@ struct CoreBf16 {
             const int ec = min(max(e, 40), 240);
             const float up = __uint_as_float((uint32_t)(268 - ec) << 23);  // 2^14 for 2^(ec - 127)
             // true q . n = 2^24 / up of the product's: 2^(ec - 117)
-            const float a_scale = e == 255 ? __uint_as_float(0x7fc00000u) : a.scale * __uint_as_float((uint32_t)(ec + 10) << 23);
-            const float unit = __uint_as_float((uint32_t)(244 - ec) << 23);         // 2^(117 - ec)
+            const float a_scale = a.scale * __uint_as_float((uint32_t)(ec + 10) << 23);
+            // 2^(117 - ec); a query that is not finite makes its scores NaN, not the scale that hidden keys' -inf meet too
+            const float unit = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(244 - ec) << 23);
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
                 sum[gr] *= unit;

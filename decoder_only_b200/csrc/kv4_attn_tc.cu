@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                         }
                     }
                 }
+                if (lim < 0) mul = 1.f;                  // sees nothing of the page: -inf times this is -inf, whatever the query
                 // scores in halves: the second half's maximum, then the first half stays for its weights
                 const bool cut = __any_sync(0xffffffffu, lim < BKV - 1);
                 float sv[64], mx8[8];

@@ -1,5 +1,6 @@
 """Attention over the 4-bit cache where numbers are not finite or scores vanish: what a row sees counts, what it does
 not see does not, and a row that sees nothing is zeros."""
+import numpy as np
 import pytest
 import torch
 
@@ -28,3 +29,23 @@ def test_a_seen_nan_value_shows_whatever_its_weight_and_wherever_the_sequence_en
     want = torch.zeros_like(o, dtype=torch.bool)
     want[..., :64] = True
     assert torch.equal(o.isnan(), want) and lb.op_last_error() == 0
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [
+    (6, 2, 64, [3, 200, 0, 10], [7, 100, 2, 0]),              # few columns
+    (4, 4, 128, [20, 0], [25, 3]),
+    (40, 8, 128, [80, 200, 20, 90], [90, 150, 60, 100]),      # many
+    (16, 16, 64, [100, 0, 300], [300, 5, 290]),
+])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_that_see_nothing_are_zeros_whatever_their_query(H, n_kv, hd, lens, new, bad, dtype):
+    c = _attend_case(H + hd, lens, new, H, n_kv, hd, dtype, poison=True)
+    good = _attend(c)
+    blind = np.zeros(len(c["q"]), bool)
+    for b, n in enumerate(new):
+        blind[c["cu"][b]:c["cu"][b] + max(n - lens[b], 0)] = True
+    c["q"][torch.from_numpy(blind).cuda()] = bad
+    o = _attend(c)
+    assert blind.any() and not o[torch.from_numpy(blind).cuda()].any()
+    assert torch.equal(o, good) and lb.op_last_error() == 0
