@@ -475,7 +475,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                         }
                     }
                 }
-                if (lim < 0) mul = 1.f;                  // sees nothing of the page: -inf times this is -inf, whatever the query
+                // hidden scores are -inf and stay so: nothing of the page is seen, whatever the query; or the query's factor
+                // and the keys' are so small that their product is 0 (scores of 0, up to 2^-97)
+                if (lim < 0 || mul == 0.f) mul = __uint_as_float(1u << 23);
                 // scores in halves: the second half's maximum, then the first half stays for its weights
                 const bool cut = __any_sync(0xffffffffu, lim < BKV - 1);
                 float sv[64], mx8[8];

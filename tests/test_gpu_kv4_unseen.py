@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import decoder_only_b200 as lb
+import _serving as ref
 from test_gpu_serving import _attend, _attend_case, _scales
 
 pytestmark = pytest.mark.gpu
@@ -37,7 +38,7 @@ def test_a_seen_nan_value_shows_whatever_its_weight_and_wherever_the_sequence_en
     (40, 8, 128, [80, 200, 20, 90], [90, 150, 60, 100]),      # many
     (16, 16, 64, [100, 0, 300], [300, 5, 290]),
 ])
-@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 0.0])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rows_that_see_nothing_are_zeros_whatever_their_query(H, n_kv, hd, lens, new, bad, dtype):
     c = _attend_case(H + hd, lens, new, H, n_kv, hd, dtype, poison=True)
@@ -49,3 +50,40 @@ def test_rows_that_see_nothing_are_zeros_whatever_their_query(H, n_kv, hd, lens,
     o = _attend(c)
     assert blind.any() and not o[torch.from_numpy(blind).cuda()].any()
     assert torch.equal(o, good) and lb.op_last_error() == 0
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [
+    (4, 2, 128, [40, 300, 0], [9, 6, 1]),                     # few columns
+    (32, 4, 128, [100, 300, 0, 0], [100, 80, 1, 0]),          # many
+    (32, 4, 64, [200, 129], [70, 129]),
+])
+@pytest.mark.parametrize("keys", [0.0, 2.0 ** -60])
+@pytest.mark.parametrize("queries", [0.0, 2.0 ** -60])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scores_that_vanish_weigh_alike(H, n_kv, hd, lens, new, keys, queries, dtype):
+    """Queries and keys that are zero, or as good as: a row is the mean of the values that it sees."""
+    c = _attend_case(H + hd, lens, new, H, n_kv, hd, dtype)
+    c["q"].mul_(queries)
+    zs, put = _scales(c, hd)
+    if keys == 0:
+        zs[..., 0, :, :] = 0
+    else:
+        zs[..., 0, :, :] -= 60 << 7                           # 2^-60 of what they were
+    put()
+    o = _attend(c).double().cpu().numpy()
+    _, V, _, _ = ref.unpack(c["pool"], hd)
+    half = 2.0 ** -9 if dtype == BF16 else 2.0 ** -24
+    for b, (length, n) in enumerate(zip(lens, new)):
+        for i in range(n):
+            seen, row = length - n + i + 1, o[c["cu"][b] + i].reshape(H, hd)
+            if seen <= 0:
+                assert not row.any()
+                continue
+            for h in range(H):
+                v = np.concatenate([V[p, h * n_kv // H] for p in c["table"][b][: -(-length // 128)]])[:seen]
+                mean, most = v.mean(0), np.abs(v).max(0)
+                # weights are one in every precision; values (many columns: fp16, 2^-12 of them next to a largest of 16
+                # times as much at most) and weights times steps (fp16 again, 31 steps) are off by half a place each
+                off = half * np.abs(mean) + (2.0 ** -6 if dtype == BF16 else 2.0 ** -18) * most
+                assert np.all(np.abs(row[h] - mean) <= off), (b, i, h)
+    assert lb.op_last_error() == 0
