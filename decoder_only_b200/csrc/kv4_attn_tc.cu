@@ -37,18 +37,26 @@
 // cost twice the output's own rounding, 3.9e-3 instead of 1.7e-3 of it), so
 // their ranges are looked after: a page's keys, and its values, are scaled by
 // the power of two that brings the page's largest to 2^10 .. 2^11, a column's
-// query likewise; scores are multiplied back in fp32, and the weights carry
-// the values' factor against the largest so far.  A code becomes 1024 + n or
+// query likewise; scores are multiplied back in fp32, and the outputs so far
+// are brought to the page's scale where that is more than 2^8 off (else the
+// weights carry the difference).  A code becomes 1024 + n or
 // 1024 + 16 n in fp16 (a mask and an or), n exactly by one operation, and
 // z + n s by one fused multiply-add with one rounding.  Scores, maxima, sums
 // and outputs are fp32.  The channels of 8 neighbours stand as c0 c4 c1 c5 c2
 // c6 c3 c7, the order in which masks take them out of a word: the queries
 // are stored in the same order, and the outputs are put back in theirs.
 //
-// In a page where some row's largest is 2^8 below the page's (outliers among
-// the keys or values), every row has a factor of its own: keys' factors go to
-// the scores, values' to the weights, relative to the largest that the column
-// sees.  So a column is not touched by the size of what it does not see.
+// Where some row's keys are 2^8 below the page's largest (outliers among
+// them), every row has a factor of its own, which goes to the scores.  A key's
+// channels share one: those 2^-24 of the key's largest and less are rounded
+// away.  Where some 64 channels of a row's values are 2^8 below the page's
+// largest, the page's values are bf16, unscaled, and its weights two bf16
+// terms, relative to the largest values that the column sees: bf16 holds any
+// size of them (their 8 bits are those of a bf16 cache).  With fp16 and a
+// factor per row, 64 channels much smaller than the row's others were lost,
+// and small values beside large ones of little weight.  So a column is not
+// touched by the size of what it does not see, nor one half of a head by that
+// of the other.
 //
 // A page outside the pool is not seen.  A group of values that holds NaN is
 // unpacked as zeros and its positions noted, and a column that sees one of
@@ -98,18 +106,19 @@ struct TCfg {
 };
 
 // Of a page: positions with NaN values per group; outside the pool; exponents
-// (biased) of its largest key and value; whether rows have their own
+// (biased) of its largest key and value; whether its keys' sizes, its values'
+// are wide apart
 struct Notes {
     uint32_t nan[2][4];
-    int bad, ke, ve, wide, pad[4];
+    int bad, ke, ve, k_wide, v_wide, pad[3];
 };
 static_assert(sizeof(Notes) == 64, "notes");
-// Of a wide page's rows: what brings a key back, and a value's exponent
+// Of a wide page's rows: what brings a key back, and the exponent of a row's largest value
 struct Rows {
     float k[PAGE], v[PAGE];
 };
 static_assert(sizeof(Rows) == 1024, "rows");
-constexpr int WIDE = 8;              // exponents between the largest rows and the smallest
+constexpr int WIDE = 8;              // exponents between the largest rows (of values: 64 channels of a row) and the smallest
 
 // Products of one 16-deep step, D (+)= A B.  Shared-memory descriptors as
 // their low words (address, leading offset): the high word is that of
@@ -143,6 +152,14 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// 16 columns of one TMEM lane per thread (warp-collective)
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -183,6 +200,75 @@ __device__ __forceinline__ void unpack_row(uint32_t tile, int r, const uint32_t 
             st_shared16(tile + gr * (128 * 128) + r * 128 + ((p ^ (r & 7)) << 4), y0, y1, y2, y3);
         }
     }
+}
+
+// The same as bf16 values, not scaled; no further from zero than the largest finite one (a call: rare, and out of the way)
+template <int GR>
+__device__ __noinline__ void unpack_row_bf16(uint32_t tile, int r, const uint32_t* w, const uint32_t* zs) {
+    constexpr float MOST = 3.38953138925153547590e38f;
+#pragma unroll 1
+    for (int gr = 0; gr < GR; ++gr) {
+        const float z = lo_bf16(zs[gr]), s = hi_bf16(zs[gr]);
+#pragma unroll 1
+        for (int p = 0; p < 8; ++p) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {        // codes i and i + 4: under the exponent of 2^23, less 2^23
+                float v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float n = __uint_as_float(((w[p * GR + gr] >> (4 * i + 16 * h)) & 15u) | 0x4b000000u) - 8388608.f;
+                    v[h] = fminf(fmaxf(fmaf(n, s, z), -MOST), MOST);
+                }
+                y[i] = pack_bf16x2(v[0], v[1]);
+            }
+            st_shared16(tile + gr * (128 * 128) + r * 128 + ((p ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+    }
+}
+
+// Rare pages stay out of the way of the others: calls, so that their registers and code do not count there.
+// A column's scores, each times what brings its key back
+__device__ __noinline__ void scores_wide(uint32_t s_addr, const float* k, float q_scale) {
+#pragma unroll 1
+    for (int c = 0; c < BKV / 32; ++c) {
+        float s[32];
+        tmem_ld32(s_addr + c * 32, s);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] *= k[32 * c + i] * q_scale;
+        tmem_st32(s_addr + c * 32, s);
+    }
+    tmem_st_wait();
+}
+// A column's weights 2^(score mul + shift), times f in two bf16 terms over the scores that they come from: 32 at a time,
+// 16 columns of first terms and 16 of second ones.  Returns their sum (without f)
+__device__ __noinline__ float weights_wide(uint32_t s_addr, int lim, float mul, float shift, float f) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < BKV / 32; ++c) {
+        float w[32];
+        tmem_ld32(s_addr + c * 32, w);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            w[i] = ex2(fmaf(i + 32 * c <= lim ? w[i] : -INFINITY, mul, shift));
+            part[i & 3] += w[i];
+            w[i] *= f;
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[i] = pack_bf16x2(w[2 * i], w[2 * i + 1]);
+                w[2 * i] -= lo_bf16(p[i]);
+                w[2 * i + 1] -= hi_bf16(p[i]);
+            }
+            tmem_st16(s_addr + c * 32 + t * 16, p);
+        }
+    }
+    return sum;
 }
 
 // Pages that the columns up to `col` (of n G) see, one at least
@@ -339,6 +425,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
         // formed in uniform registers, where the products take them from
         constexpr uint32_t IDESC_QK = idesc_f16(BKV);                  // K-major A and B
         constexpr uint32_t IDESC_PV = idesc_f16(HD) | (1u << 16);      // B (V) MN-major
+        constexpr uint32_t IDESC_PV_WIDE = idesc_bf16(HD) | (1u << 16);
         const int x = __shfl_sync(0xffffffffu, warp, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t d_s = tm + 128u * x, d_o = tm + 256u + 128u * x;    // P over S
@@ -375,14 +462,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                     if (j == nk - 1) umma_commit(q_empty);
                 }
                 __syncwarp();
+                const bool wide = __shfl_sync(0xffffffffu, notes[kv % NF].v_wide, 0);       // there since k_full
                 ok = wait(v_full + 8 * st, use) && (!seen || wait(p_full + 8 * x, c)) && (j > 0 || !seen || nix == 0 || wait(o_free + 8 * x, nix - 1));
                 if (!ok) break;
                 if (one) {
                     if (seen) {
                         tc_fence_after();
                         const uint32_t v_lo = desc_lo(sV + st * C::TILE, C::REG >> 4);                 // lead: the next 64 channels
+                        if (wide) {                                                                    // 32 weights' first terms, their second
 #pragma unroll
-                        for (int kk = 0; kk < BKV / 16; ++kk) umma_ts(d_o, d_s + 8u * kk, v_lo + kk * (2048u >> 4), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < 2 * (BKV / 16); ++kk)
+                                umma_ts(d_o, d_s + 32u * (kk >> 2) + 8u * ((kk >> 1) & 1) + 16u * (kk & 1), v_lo + (kk >> 1) * (2048u >> 4),
+                                        IDESC_PV_WIDE, (j > 0 || kk > 0) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < BKV / 16; ++kk) umma_ts(d_o, d_s + 8u * kk, v_lo + kk * (2048u >> 4), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                        }
                         umma_commit(pv_done + 8 * x);
                         if (j == n - 1) umma_commit(o_last + 8 * x);
                     }
@@ -436,7 +531,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
             }
             const int pos = im.sq.len - im.sq.n + (there ? gc / a.G : 0);      // sees positions 0 .. pos
             float m = -INFINITY, l = 0.f, poison[2] = {0.f, 0.f};
-            int ve = 0;                                  // exponent that the outputs so far are scaled for
+            int ve = 0, vtop = 0;                        // exponent that the outputs so far are scaled for, and the largest seen
             for (int j = 0; j < im.n(x); ++j, ++sc) {
                 if (!__all_sync(0xffffffffu, mbar_wait(s_full + 8 * x, (uint32_t)(sc & 1), abort_flag, a.err))) {
                     ok = false;
@@ -447,20 +542,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 const int lim = note.bad ? -1 : min(pos, im.sq.len - 1) - (im.j0 + j) * PAGE;   // last position of the page that is seen
                 float mul = q_scale * from_2_10(note.ke);
                 int page_ve = note.ve;
-                if (note.wide) {                         // of the values that the column sees; scores brought back here
-                    const Rows& own = rows[(kv0 + j) % NF];
-                    mul = 1.f;
+                const bool v_wide = note.v_wide;
+                const Rows& own = rows[(kv0 + j) % NF];
+                if (v_wide) {                            // of the values that the column sees
                     page_ve = 0;
                     for (int i = 0; i <= lim && i < BKV; ++i) page_ve = max(page_ve, (int)own.v[i]);
-#pragma unroll 1
-                    for (int c = 0; c < BKV / 32; ++c) {
-                        float s32[32];
-                        tmem_ld32(s_addr + c * 32, s32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s32[i] *= own.k[32 * c + i] * q_scale;
-                        tmem_st32(s_addr + c * 32, s32);
-                    }
-                    tmem_st_wait();
+                }
+                if (note.k_wide) {                       // scores brought back here
+                    mul = 1.f;
+                    scores_wide(s_addr, own.k, q_scale);
                 }
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
@@ -510,18 +600,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                     m = mt;
                     rescale = true;
                 }
-                // the values' factor: 2^(10 - page_ve) in them, so the weights carry 2^(page_ve - ve) <= 1; a larger
-                // page scales the outputs so far down (all columns alike)
-                float down = 1.f;
-                if (page_ve > ve) {
-                    down = ve == 0 ? 1.f : exp2f((float)(ve - page_ve));
-                    ve = page_ve;
-                    rescale |= down != 1.f;
+                // the values' factor: 2^(10 - page_ve) in them, so the weights carry 2^(page_ve - ve), 2^-8 .. 1: a page of
+                // values of another size scales the outputs so far (fp32), up by 2^60 at most, instead of its weights (fp16)
+                float resize = 1.f;
+                if (page_ve > ve || (page_ve < ve - WIDE && page_ve > 0)) {
+                    vtop = max(vtop, page_ve);
+                    const int unit = max(page_ve, vtop - 60);
+                    resize = ve == 0 ? 1.f : exp2f((float)(ve - unit));
+                    ve = unit;
+                    rescale |= resize != 1.f;
                 }
+                const float shift = m == -INFINITY ? 0.f : -m;
                 // past 2^-40 the page adds nothing, but to the sum of weights
-                const float carry = note.wide ? 0.f : (float)max(page_ve - ve, -40);
-                const float minus = (m == -INFINITY ? 0.f : -m) + carry;
+                const float carry = v_wide ? 0.f : (float)max(page_ve - ve, -40);
+                const float minus = shift + carry;
                 float rs4[4] = {0.f, 0.f, 0.f, 0.f};
+                if (v_wide) {                            // values in bf16, weights in two terms of it: they bring any value to the outputs' scale
+                    rs4[0] = weights_wide(s_addr, lim, mul, shift, ve == 0 ? 0.f : to_2_10(ve));     // 0: nothing seen so far
+                } else
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (half == 1) load(1, false);
@@ -543,22 +639,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 }
                 const float rs = (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
                 tmem_st_wait();
-                if (note.wide) {                         // each weight times its value's factor (a power of two, at most 1)
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float p32[32];
-                        tmem_ld32(s_addr + c * 32, p32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&p32[i]));
-                            const float* vx = rows[(kv0 + j) % NF].v + 64 * c + 2 * i;
-                            p32[i] = __uint_as_float(pack_f16x2(w.x * ex2(fminf(fmaxf(vx[0] - (float)ve, -40.f), 0.f)),
-                                                                w.y * ex2(fminf(fmaxf(vx[1] - (float)ve, -40.f), 0.f))));
-                        }
-                        tmem_st32(s_addr + c * 32, p32);
-                    }
-                    tmem_st_wait();
-                }
                 // a warp with a moved maximum rescales its rows of O_x: the previous P_x V has completed
                 // (S_x(j) was issued after it)
                 if (__any_sync(0xffffffffu, rescale)) {
@@ -567,7 +647,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                         float ov[32];
                         tmem_ld32(o_addr + c * 32, ov);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] *= corr * down;
+                        for (int i = 0; i < 32; ++i) ov[i] *= corr * resize;
                         tmem_st32(o_addr + c * 32, ov);
                     }
                     tmem_st_wait();
@@ -704,7 +784,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 page = page_of(j + 2);
                 ok = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, par, abort_flag, a.err));
                 if (!ok) break;
-                uint32_t kt_top = 0, vt_top = 0;         // bits of |z| + 15 s, which no value passes
+                uint32_t kt_top = 0, vt_top = 0, vt_least = ~0u;     // bits of |z| + 15 s, which no value passes
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
                     const unsigned nan = __ballot_sync(0xffffffffu, not_finite(nz[gr]));
@@ -712,10 +792,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                     if (lane == 0) notes[kt % NF].nan[gr][r / 32] = nan;
                     if (!not_finite(z[gr])) kt_top = max(kt_top, __float_as_uint(fabsf(lo_bf16(z[gr])) + 15.f * hi_bf16(z[gr])));
                     else z[gr] = 0x7fc07fc0u;
-                    vt_top = max(vt_top, __float_as_uint(fabsf(lo_bf16(nz[gr])) + 15.f * hi_bf16(nz[gr])));
+                    const uint32_t v = __float_as_uint(fabsf(lo_bf16(nz[gr])) + 15.f * hi_bf16(nz[gr]));
+                    vt_top = max(vt_top, v);
+                    vt_least = min(vt_least, v - 1u);                // not of zeros
                 }
                 const uint32_t k_max = __reduce_max_sync(0xffffffffu, kt_top), v_max = __reduce_max_sync(0xffffffffu, vt_top);
-                const uint32_t k_min = __reduce_min_sync(0xffffffffu, kt_top - 1u), v_min = __reduce_min_sync(0xffffffffu, vt_top - 1u);  // not of zeros
+                const uint32_t k_min = __reduce_min_sync(0xffffffffu, kt_top - 1u), v_min = __reduce_min_sync(0xffffffffu, vt_least);
                 uint32_t* top = tops + (kt & 1) * 16;
                 if (lane == 0) {
                     top[r / 32] = k_max;
@@ -727,27 +809,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 ok = __all_sync(0xffffffffu, mbar_wait(bars + B_TOPS, (uint32_t)(kt & 1), abort_flag, a.err));   // all four warps'
                 if (!ok) break;
                 int ke = exponent(max(max(top[0], top[1]), max(top[2], top[3])));
-                int vee = exponent(max(max(top[4], top[5]), max(top[6], top[7])));
-                const bool wide = exponent(min(min(top[8], top[9]), min(top[10], top[11]))) < ke - WIDE ||
-                                  exponent(min(min(top[12], top[13]), min(top[14], top[15]))) < vee - WIDE;
+                const int vee = exponent(max(max(top[4], top[5]), max(top[6], top[7])));
+                const bool k_wide = exponent(min(min(top[8], top[9]), min(top[10], top[11]))) < ke - WIDE;
+                const bool v_wide = exponent(min(min(top[12], top[13]), min(top[14], top[15]))) < vee - WIDE;
                 if (r == 0) {
                     notes[kt % NF].bad = now_bad;
                     notes[kt % NF].ke = ke;
                     notes[kt % NF].ve = vee;
-                    notes[kt % NF].wide = wide;
+                    notes[kt % NF].k_wide = k_wide;
+                    notes[kt % NF].v_wide = v_wide;
                 }
-                if (wide) {
+                if (k_wide) {
                     ke = exponent(kt_top);
-                    vee = exponent(vt_top);
                     rows[kt % NF].k[r] = from_2_10(ke);
-                    rows[kt % NF].v[r] = (float)vee;
                 }
+                if (v_wide) rows[kt % NF].v[r] = (float)exponent(vt_top);
                 unpack_row<GR>(sK + st * C::TILE, r, w, z, to_2_10(ke));
                 fence_async();
                 mbar_arrive(k_full + 8 * st);
                 ok = __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * st, par, abort_flag, a.err));
                 if (!ok) break;
-                unpack_row<GR>(sV + st * C::TILE, r, nv, nz, to_2_10(vee));
+                if (v_wide) {
+                    uint32_t wv[8 * GR], wz[GR];
+#pragma unroll
+                    for (int i = 0; i < 8 * GR; ++i) wv[i] = nv[i];
+#pragma unroll
+                    for (int i = 0; i < GR; ++i) wz[i] = nz[i];
+                    unpack_row_bf16<GR>(sV + st * C::TILE, r, wv, wz);
+                } else {
+                    unpack_row<GR>(sV + st * C::TILE, r, nv, nz, to_2_10(vee));
+                }
                 fence_async();
                 mbar_arrive(v_full + 8 * st);
             }

@@ -537,7 +537,10 @@ LLAMA_API int llama_op_kv4_read(int32_t dtype, const void* d_pool, const int32_t
  * LLAMA_F32: products at fp32 accuracy.  LLAMA_BF16: queries and weights as
  * fp16 (11 bits) next to powers of two that follow their size; for a request
  * with more than 240 rows times heads of a group, and all of a call whose work
- * is mostly such requests, z + n s is rounded to fp16 too.  What
+ * is mostly such requests, z + n s is rounded to fp16 too (values of sizes far
+ * apart to bf16; a key's channels 2^-24 of its largest are lost).  For the
+ * others a weight times a step counts down to 2^-24 of the largest step of
+ * the 64 channels that the row sees.  What
  * a row does not see (later tokens, whatever lies behind a sequence) may hold
  * anything, NaN too; a NaN key that it does see makes its head NaN, a NaN
  * value the 64 channels.  Sums are formed before they are divided: values past

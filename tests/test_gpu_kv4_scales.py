@@ -1,0 +1,71 @@
+"""Attention over the 4-bit cache against 64 bits, by the error of each head (or of 64 channels of one) relative to its
+norm, where values differ in size between channels, positions and pages."""
+import numpy as np
+import pytest
+import torch
+
+import decoder_only_b200 as lb
+import _serving as ref
+from test_gpu_serving import FUTURE, MANY, _attend, _attend_case, _scales
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _errors(c, got, width):
+    """|got - want| / |want| of every `width` channels of every row, by norms; [rows, H * hd / width]."""
+    want, _ = ref.attention(c["q64"], c["pool"], c["table"], c["lens"], c["cu"], c["n_kv"], False)
+    want = want.reshape(len(want), -1, width)
+    off = got.double().cpu().numpy().reshape(want.shape) - want
+    size = np.linalg.norm(want, axis=-1)
+    none = size == 0                                          # rows that see nothing
+    assert not off[none].any()
+    return np.where(none, 0.0, np.linalg.norm(off, axis=-1) / np.where(none, 1.0, size))
+
+
+# Roundings to nearest of independent numbers, each 2^-p at the most and a 1.7th of it on average: the output to bf16
+# (p = 9), 2^-9.8; weights times steps or keys, values and weights in fp16 (p = 12), which against codes that all have
+# one sign weigh twice, 2^-10.8 a time: below 2^-9 together.  Twice that for one head of thousands.
+FINE = 2.0 ** -8
+# A page whose values differ widely in size takes weights and values in bf16 (p = 9 each, about the size of the output's own
+# rounding): below 2^-8.5 together, doubled again
+WIDE = 2.0 ** -7.5
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [s for s in FUTURE if s[2] == 128] + [(16, 8, 128, [700, 260], [130, 256])])
+@pytest.mark.parametrize("group", [0, 1])
+@pytest.mark.parametrize("power", [-60, -36, -24, -12, 12, 24, 36])
+@pytest.mark.parametrize("where", ["all", "some", "first page", "last page"])
+def test_attention_with_64_channels_of_the_values_of_another_size(H, n_kv, hd, lens, new, group, power, where):
+    """One group's values 2^power times as large: at every position, at a third of them, in the first or the last page."""
+    c = _attend_case(H + hd + 2, lens, new, H, n_kv, hd, BF16)
+    zs, put = _scales(c, hd)
+    rng = np.random.default_rng(3)
+    for b, length in enumerate(lens):
+        for pos in range(length):
+            if {"all": True, "some": rng.random() < 0.33, "first page": pos < 128, "last page": pos // 128 == (length - 1) // 128}[where]:
+                zs[c["table"][b, pos // 128], :, pos % 128 // 32, 1, pos % 32, group] += (power << 7) & 0xffff
+    put()
+    e = _errors(c, _attend(c), 64)
+    print("largest error", e.max())
+    assert e.max() <= WIDE, e.max()
+    assert lb.op_last_error() == 0
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [s for s in FUTURE if s[2] == 128])
+@pytest.mark.parametrize("group", [0, 1])
+@pytest.mark.parametrize("power", [-60, 30, 100, None])
+def test_attention_rows_do_not_depend_on_64_channels_that_come_after_them(H, n_kv, hd, lens, new, group, power):
+    c = _attend_case(H + hd + 3, lens, new, H, n_kv, hd, BF16)
+    zs, put = _scales(c, hd)
+    for b, length in enumerate(lens):
+        for pos in (length - 2, length - 1):
+            at = zs[c["table"][b, pos // 128], :, pos % 128 // 32, 1, pos % 32, group]
+            at[:] = 0x7fc0 if power is None else at + ((power << 7) & 0xffff)
+    put()
+    out = _attend(c)
+    rows = np.concatenate([np.arange(c["cu"][b], c["cu"][b + 1] - 2) for b in range(len(lens))])
+    e = _errors(c, out, 64)[rows]
+    print("largest error", e.max())
+    assert e.max() <= WIDE, e.max()
