@@ -69,3 +69,43 @@ def test_attention_rows_do_not_depend_on_64_channels_that_come_after_them(H, n_k
     e = _errors(c, out, 64)[rows]
     print("largest error", e.max())
     assert e.max() <= WIDE, e.max()
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", MANY + [
+    (32, 8, 128, [2014, 1381, 777], [384, 448, 1]), (14, 2, 64, [129, 900], [129, 200]), (5, 1, 64, [400], [400]),
+    (4, 4, 128, [40, 300, 1], [9, 6, 1]), (9, 3, 64, [70, 33, 500], [8, 3, 1]),           # few columns
+    (8, 1, 128, [9001], [1]), (12, 12, 64, [33, 2000, 5], [1, 1, 1]),
+])
+def test_attention_error_relative_to_each_head(H, n_kv, hd, lens, new):
+    c = _attend_case(H + hd + 4, lens, new, H, n_kv, hd, BF16, poison=True, strided=True)
+    e = _errors(c, _attend(c), hd)
+    print("largest error", e.max(), "rms", np.sqrt((e ** 2).mean()))
+    assert e.max() <= FINE, e.max()
+    assert lb.op_last_error() == 0
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [(32, 4, 128, [100, 300], [100, 80]), (16, 16, 64, [700, 300], [250, 300]),
+                                                (8, 2, 128, [300, 40], [9, 3]), (6, 6, 64, [513], [1])])
+@pytest.mark.parametrize("sharp", [4.0, 16.0])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_error_of_peaked_softmax(H, n_kv, hd, lens, new, sharp, dtype):
+    """Queries that are keys of their sequence, so that a few positions hold nearly all of the weight and the running
+    maximum moves.  A score's error moves a weight in proportion: scores of sharp * sqrt(hd) and less, of which fp16
+    (many columns: queries and keys, 2^-12 each and independent over hd channels) gets 2^-11.5 / 1.7 / sqrt(hd) of |q||k|
+    wrong, under sharp * 2^-12 of 1; fp32's products 2^-20."""
+    rng = np.random.default_rng(9)
+    c = _attend_case(H + hd + 5, lens, new, H, n_kv, hd, dtype)
+    K, _, _, _ = ref.unpack(c["pool"], hd)
+    G = H // n_kv
+    q = np.zeros((len(c["q"]), H, hd))
+    for b, (length, n) in enumerate(zip(lens, new)):
+        for i in range(n):
+            for h in range(H):
+                pos = rng.integers(0, length - n + i + 1)
+                k = K[c["table"][b, pos // 128], h // G, pos % 128]
+                q[c["cu"][b] + i, h] = sharp * np.sqrt(hd) / np.linalg.norm(k) ** 2 * k
+    t = torch.from_numpy(q).to(dtype)
+    c["q"], c["q64"] = t.cuda(), t.double().numpy()
+    e = _errors(c, _attend(c), hd)
+    print("largest error", e.max(), "rms", np.sqrt((e ** 2).mean()))
+    assert e.max() <= (FINE + sharp * 2.0 ** -11 if dtype == BF16 else 2.0 ** -18), e.max()
