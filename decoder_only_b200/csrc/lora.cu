@@ -56,7 +56,9 @@ struct Tile {
 };
 __device__ __forceinline__ Tile tile_of(const LoraArgs& a, int i) {
     Tile t{0, 0, 0};
-    if (i >= min(*a.n_tiles, a.max_tiles)) return t;
+    const int n = *a.n_tiles;
+    if (n < 0 || n > a.max_tiles) atomicOr(a.err, LLAMA_DEVERR_INPUT);
+    if (i >= min(n, a.max_tiles)) return t;
     const int4 v = a.tiles[i];
     if (v.x < 0 || v.x >= a.n_adapters || v.z < 0 || v.z > LLAMA_LORA_TILE || v.y < 0 || v.y > a.M - v.z) {
         atomicOr(a.err, LLAMA_DEVERR_INPUT);
