@@ -527,13 +527,16 @@ def batch_plan(past: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free:
                out: BatchPlan | None = None) -> BatchPlan:
     """Plans a step on the device (llama_op_batch_plan).  past, new [B]; table
     [B, pages_per_seq], updated in place; free [capacity] and n_free [1], the
-    stack of free pages.  `out` reuses a plan's buffers; past may then be its
-    kv_len and n_free its n_free (the step after)."""
+    stack of free pages.  `out` reuses a plan's buffers (and takes max_rows and
+    n_adapters from it); past may then be its kv_len and n_free its n_free (the
+    step after)."""
     B = past.numel()
     if out is None:
         _need(max_rows is not None, "batch_plan: max_rows or out")
         _here("batch_plan", past)
         out = BatchPlan(B, max_rows, n_adapters)
+    else:
+        _need(max_rows in (None, out.max_rows) and n_adapters in (0, out.n_adapters), "batch_plan: out is of another max_rows or n_adapters")
     stream = _here("batch_plan", past, new, table, free, n_free, adapter, out.cu)
     _i32("batch_plan", past, new, table, free, n_free, adapter)
     _need(out.batch == B and new.numel() == B and table.dim() == 2 and table.shape[0] == B and n_free.numel() == 1,
@@ -606,8 +609,10 @@ def attention_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, kv_l
                   max_q: int = 1, out: torch.Tensor | None = None, work: torch.Tensor | None = None) -> torch.Tensor:
     """q [rows, H, head_dim] over the 4-bit cache -> o [rows, H * head_dim]
     (llama_op_attention_kv4).  Request b has kv_len[b] positions and the rows
-    cu[b] .. cu[b + 1] - 1 (at most max_q; cu None: one row each).  Rows of no
-    request are left as they were in `out` (uninitialised without it)."""
+    cu[b] .. cu[b + 1] - 1 (cu None: one row each).  max_q has to be the most rows
+    of a request or more: a request with more is left out, which op_last_error
+    reports.  Rows of no request are left as they were in `out` (uninitialised
+    without it)."""
     _need(q.dim() == 3, "attention_kv4: q")
     rows, H, hd = q.shape
     n_pages, n_kv = _pool_shape("attention_kv4", pool, hd)
