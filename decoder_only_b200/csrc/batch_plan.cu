@@ -8,8 +8,8 @@
 // binary search in those sums.  The work is a few kilobytes: latency bounds
 // it.  Up to FUSED_ROWS rows the same CTA fills them too (one launch); past
 // that a second kernel spreads the rows over the SMs.  64 requests, 8
-// adapters, 512, 2048, 4096 and 16384 rows: 4.0, 5.7, 7.4 and 17.1 us in the
-// one CTA, 5.3, 6.1, 6.1 and 5.9 us with the second kernel.
+// adapters, 512, 2048, 4096 and 16384 rows: 5.0, 5.8, 6.9 and 11.1 us in the
+// one CTA, 6.4, 6.2, 6.4 and 6.2 us with the second kernel.
 //
 // Sums saturate at 2^31 - 1: saturating addition of non-negative numbers is
 // associative, and every capacity they are compared with is smaller.

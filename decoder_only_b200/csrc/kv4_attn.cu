@@ -24,9 +24,11 @@
 // 16.0, then n - 7.5 by one subtraction, so that sums stay short.
 //
 // Bound: HBM (144 bytes per position and key/value head at head_dim 128) in
-// principle; in fact the instructions issued per unit (660 per warp at head_dim
-// 128), above all on the integer pipe.  32 sequences x 40 heads x up to 2304
-// positions: 76 us, 4.2 TB/s (the bytes alone: 49 us; issue slots 58% busy);
+// principle; in fact nothing is full (HBM 64% of the copy rate, issue slots and
+// integer pipe 58%): the 16 warps of an SM, all that 128 registers a thread
+// leave room for, do not cover the fixed latencies of the 660 instructions that
+// a unit takes a warp at head_dim 128.  32 sequences x 40 heads x up to 2304
+// positions: 77 us, 4.2 TB/s (the bytes alone: 49 us);
 // 131071 positions, 64 heads on 8: 46 us (23 us), 8 of them the join.  With
 // codes turned into bf16 16 + n by three instructions per operand instead of
 // one mask the former took 109 us.  A query column is one (token, head) of a

@@ -4,7 +4,7 @@
 // A query column is a (token, head) pair of a key/value head's group; 128 of
 // them fill a tile.  Per tile: O = softmax(Q K^T / sqrt(hd) + causal mask) V
 // over the pages the tile's last token sees, with K = z + n s and V alike
-// turned into bf16 tiles in shared memory as they are needed, so a page is
+// turned into fp16 tiles in shared memory as they are needed, so a page is
 // unpacked once for 256 columns (two adjacent tiles of an item) instead of
 // once for 16 as in the kernel for few columns (kv4_attn.cu).
 //
@@ -92,7 +92,7 @@ constexpr int B_OLAST = B_PVDONE + 16, B_OFREE = B_OLAST + 16, B_DRAIN = B_OFREE
 
 template <int HD>
 struct TCfg {
-    static constexpr int REG = 128 * 128;            // [128 rows][64 bf16], 128-byte swizzle
+    static constexpr int REG = 128 * 128;            // [128 rows][64 numbers of 16 bits], 128-byte swizzle
     static constexpr int NREG = HD / 64;
     static constexpr int TILE = NREG * REG;
     static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NS * TILE, OFF_BAR = OFF_V + NS * TILE;

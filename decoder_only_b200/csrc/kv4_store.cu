@@ -34,7 +34,8 @@ namespace {
 constexpr int THREADS = 128;         // append and read as above: 73 us, with 64 and 256 threads 81 and 76
 constexpr int PER = 16;              // channels per thread
 
-// n / d for n < 2^31 by a product and a shift
+// n / d for n < 2^31 by a product and a shift (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994)
 struct FastDiv {
     uint32_t d, m, l;
     explicit FastDiv(uint32_t div) : d(div), l(0) {

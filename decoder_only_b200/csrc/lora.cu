@@ -552,7 +552,8 @@ int run(bool is_bf16, LoraArgs& a, cudaStream_t st) {
     // every CTA of a tile adds the slices again, so a tile gets as many CTAs as fill the SMs four times, and in bf16 each
     // at least two steps, the second's B on its way beside the first (24 tiles, n 5120: 24.7 us for the whole operator,
     // twice: 26.2, once: 33.5; one step of 32 rows on 16 adapters, n 4096: 10.4 us against 9.3).  fp32: twice, one CTA
-    // per SM at a time (18 tiles, n 5120: 55.5 us, four times: 57.9; 9 tiles, n 1024: 21.0, two steps each: 28.3)
+    // per SM at a time (24 tiles of rank 8, 2048 x 5120: 28.8 us, once: 37.8; 18 tiles of rank 64, 5120 x 5120: 127 us,
+    // once: 116, four times: 122; 9 tiles, 1024 x 1024: 23.0, two steps each: 31.7)
     const int cols = ceil_div(a.n, is_bf16 ? BLOCK : COLS), fill = (is_bf16 ? 4 : 2) * 148;
     const int want = a.max_tiles < fill ? fill / a.max_tiles : 1;
     a.steps = ceil_div(cols, want < cols ? want : cols);
