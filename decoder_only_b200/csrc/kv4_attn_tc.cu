@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 if (v_wide) {                            // of the values that the column sees
                     page_ve = 0;
                     for (int i = 0; i <= lim && i < BKV; ++i) page_ve = max(page_ve, (int)own.v[i]);
+                    __syncwarp();                        // as many as a lane sees: together again for tensor memory
                 }
                 if (note.k_wide) {                       // scores brought back here
                     mul = 1.f;
