@@ -84,6 +84,7 @@ constexpr int SOFT0 = 2, UNPACK0 = 10;
 constexpr int NS = 2;                // stages of the key and value rings
 constexpr int NF = 4;                // pages whose notes are kept
 constexpr float RESCALE_LOG2 = 8.f;  // move the running maximum only by more than this
+constexpr float LIFT = 128.f, LIFT_LOG2 = 7.f;     // weights as fp16 are lifted to the end of its range: 2^15, and 11 bits down to 2^-21
 constexpr int ITEM = 2 * BQ;         // columns of an item
 
 constexpr int B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = B_KFULL + 8 * NS, B_VFULL = B_KEMPTY + 8 * NS;
@@ -613,11 +614,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 }
                 const float shift = m == -INFINITY ? 0.f : -m;
                 // past 2^-40 the page adds nothing, but to the sum of weights
-                const float carry = v_wide ? 0.f : (float)max(page_ve - ve, -40);
+                const float carry = v_wide ? 0.f : (float)max(page_ve - ve, -40) + LIFT_LOG2;
                 const float minus = shift + carry;
                 float rs4[4] = {0.f, 0.f, 0.f, 0.f};
                 if (v_wide) {                            // values in bf16, weights in two terms of it: they bring any value to the outputs' scale
-                    rs4[0] = weights_wide(s_addr, lim, mul, shift, ve == 0 ? 0.f : to_2_10(ve));     // 0: nothing seen so far
+                    rs4[0] = weights_wide(s_addr, lim, mul, shift, ve == 0 ? 0.f : to_2_10(ve) * LIFT);     // 0: nothing seen so far
                 } else
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) kv4_attn_tc_kernel(const __grid_c
                 tc_fence_after();
             }
             // to the output if this CTA has all of the item, else as a part: its beginning in slot 1, else in slot 0
-            const float back = (whole ? inverse(l) : 1.f) * (ve == 0 ? 1.f : from_2_10(ve));
+            const float back = (whole ? inverse(l) : 1.f) * (ve == 0 ? 1.f : from_2_10(ve) * (1.f / LIFT));
             bf16* dst = static_cast<bf16*>(a.o) + row * ((int64_t)a.H * HD) + (int64_t)qh * HD;
             float* part = tc_parts(a) + ((size_t)blockIdx.x * 2 + (im.j0 == 0)) * part_floats(HD);
             const int col = x * BQ + t_row;

@@ -109,3 +109,36 @@ def test_attention_error_of_peaked_softmax(H, n_kv, hd, lens, new, sharp, dtype)
     e = _errors(c, _attend(c), hd)
     print("largest error", e.max(), "rms", np.sqrt((e ** 2).mean()))
     assert e.max() <= (FINE + sharp * 2.0 ** -11 if dtype == BF16 else 2.0 ** -18), e.max()
+
+
+@pytest.mark.parametrize("H,n_kv,hd,lens,new", [(32, 4, 128, [100, 700], [100, 300]), (16, 16, 64, [700, 300], [250, 300]),
+                                                (8, 2, 128, [300, 40], [9, 3]), (6, 6, 64, [513], [1])])
+@pytest.mark.parametrize("bits", [12, 20])
+def test_attention_beside_a_position_that_takes_the_weight_and_gives_nothing(H, n_kv, hd, lens, new, bits):
+    """A first position of zero values whose score is about `bits` above the others' in base 2: what is left of the weights
+    makes the result.  fp16 rounds what is below 2^-14 to multiples of 2^-24, by 2^-25 at the most: with many columns 2^7
+    times a weight, so 2^-32 of its value; with few 2^5 times a weight and more times its step over the largest step, so
+    2^-30 of the largest step, and that for up to 15 of them, below 2^-29 of the largest value (|z| is half of 15 steps
+    here).  Scores vary by several bits (rows of few positions may have weights of 2^-30 alone), so that is added to the
+    relative bound: 2^-29 of the largest value for each position, in the norm of hd channels."""
+    c = _attend_case(H + hd + 6, lens, new, H, n_kv, hd, BF16)
+    q = c["q"].abs()
+    c["q"], c["q64"] = q, q.double().cpu().numpy()
+    zs, put = _scales(c, hd)
+    # |q| has 0.8 hd as its sum: a key of z everywhere has a score of 0.8 sqrt(hd) z log2(e) in base 2
+    z = torch.tensor(bits / (0.8 * hd ** 0.5 * 1.4427), dtype=BF16).view(torch.int16).item()
+    for b in range(len(lens)):
+        at = zs[c["table"][b, 0], :, 0, :, 0]             # [heads, keys or values, groups, (z, s)]
+        at[:, 0] = [z, 0]
+        at[:, 1] = 0
+    put()
+    e = _errors(c, _attend(c), hd)
+    first = [c["cu"][b] for b in range(len(lens)) if new[b] == lens[b]]      # rows that see that position alone: zeros
+    assert not e[first].any()
+    print("largest error", e.max(), "rms", np.sqrt((e ** 2).mean()))
+    want, _ = ref.attention(c["q64"], c["pool"], c["table"], c["lens"], c["cu"], n_kv, False)
+    _, V, _, _ = ref.unpack(c["pool"], hd)
+    size = np.linalg.norm(want.reshape(e.shape + (hd,)), axis=-1)
+    seen = np.concatenate([length - n + 1 + np.arange(n) for length, n in zip(lens, new)])[:, None]
+    bound = WIDE * size + seen * 2.0 ** -29 * np.abs(V).max() * hd ** 0.5
+    assert np.all(e * size <= bound), (e * size / bound).max()
