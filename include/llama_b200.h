@@ -541,9 +541,9 @@ LLAMA_API int llama_op_kv4_read(int32_t dtype, const void* d_pool, const int32_t
  * apart to bf16; a key's channels 2^-24 of its largest are lost).  For the
  * others a weight times a step counts down to 2^-24 of the largest step of
  * the 64 channels that the row sees.  Weights lose bits below 2^-19 of a row's
- * largest and count down to 2^-29 of it.  What a row does not see (later tokens, whatever lies behind a sequence) may hold
- * anything, NaN too; a NaN key that it does see makes its head NaN, a NaN
- * value the 64 channels.  Sums are formed before they are divided: values past
+ * largest and count down to 2^-29 of it.  What a row does not see (later
+ * tokens, whatever lies behind a sequence) may hold anything, NaN too; a NaN
+ * key that it does see makes its head NaN, a NaN value the 64 channels.  Sums are formed before they are divided: values past
  * 2^100 may overflow.  Results do not depend on the run, but their last bits
  * may on the other requests of the call.  d_work:
  * llama_op_attention_kv4_work_bytes, 16-byte aligned, need not be cleared. */
